@@ -284,6 +284,18 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw64(uint32_t saddr) {
   return d;
 }
 
+// The same for the 32-byte swizzle layout: rows of 32 bytes, 8-row groups 256 bytes apart, 16-byte
+// chunk c of row r stored at chunk (c ^ ((r / 4) % 2)); the tile base is 256-byte aligned.
+__device__ __forceinline__ uint64_t desc_kmajor_sw32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address, bits 0-13
+  d |= (uint64_t)1 << 16;                     // leading byte offset (unused here), bits 16-29
+  d |= (uint64_t)(256 >> 4) << 32;            // stride byte offset, bits 32-45
+  d |= (uint64_t)1 << 46;                     // descriptor version for sm_100, bits 46-47
+  d |= (uint64_t)6 << 61;                     // layout: 32-byte swizzle, bits 61-63
+  return d;
+}
+
 // Instruction descriptor of kind::f16 with f16 A and B, f32 accumulator,
 // both operands K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
@@ -333,6 +345,23 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf_a, int sf
          | ((uint32_t)(sf_a & 3) << 29);    // A scale-factor byte
 }
 
+// Instruction descriptor of kind::mxf8f6f4 (block_scale, scale_vec::1X): E4M3 A and B, one
+// UE8M0 scale factor per row and 32 elements along K, f32 accumulator, shape M x N; a_mn / b_mn as
+// in idesc_e4m3_f32.  sf_a / sf_b (0 .. 3) pick the scale byte in each 32-bit tensor-memory column
+// that this instruction's K = 32 uses.
+__host__ __device__ constexpr uint32_t idesc_mxe4m3(int M, int N, bool a_mn, bool b_mn, int sf_a,
+                                                    int sf_b) {
+  return ((uint32_t)(sf_b & 3) << 4)        // B scale-factor byte
+         | (0u << 7)                        // A format: E4M3
+         | (0u << 10)                       // B format: E4M3
+         | ((a_mn ? 1u : 0u) << 15)         // A major
+         | ((b_mn ? 1u : 0u) << 16)         // B major
+         | ((uint32_t)(N >> 3) << 17)       // N / 8
+         | (1u << 23)                       // scale format: UE8M0
+         | ((uint32_t)(M >> 4) << 24)       // M / 16
+         | ((uint32_t)(sf_a & 3) << 29);    // A scale-factor byte
+}
+
 // Shared-memory descriptor of a scale-factor block for tcgen05.cp 32x128b:
 // 32 rows of 16 bytes, contiguous (no swizzle; 8-row groups 128 bytes apart).
 __device__ __forceinline__ uint64_t desc_sf_rows16(uint32_t saddr) {
@@ -367,6 +396,20 @@ __device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// D[tmem] (+)= (A * 2^sfA) * (B * 2^sfB)^T, E4M3 operands from shared memory (K = 32 per
+// instruction), scale factors from tensor memory.
+__device__ __forceinline__ void mma_mxe4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
+      "r"(accumulate)
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc]^T with 8-bit operands (A in tensor memory:
 // row i of A in lane i, four consecutive K elements per 32-bit column).
 __device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -391,6 +434,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {

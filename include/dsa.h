@@ -445,8 +445,11 @@ int dsa_sparse_mla_decode_nvfp4(const void* q, int H, float softmax_scale,
  * A row with row_len 0 gets out = 0 and lse = -inf.  Rows of one request that are
  * adjacent in the row order share each read of the latents.  What is behind a
  * row's row_len (NaN codes included) does not reach it; a NaN within it, or a
- * query that is not finite, gives NaN.  Results do not depend on timing, but the cut of the
- * context follows all rows of the call.
+ * query that is not finite, gives NaN.  Weights are rounded to f16 (2^-11) and to 2^-9 of
+ * themselves or 2^-17 of the largest of their 32 tokens (positions 32 i .. 32 i + 31), so
+ * whatever their distribution an output is off by at most 2^-8 of the largest |L| of its dim
+ * (and fp32 sums: 2^-21 a page) besides its own rounding; lse takes them in fp32.  Results do
+ * not depend on timing, but the cut of the context follows all rows of the call.
  *
  *  q       bf16 [R][H][576], 16-byte aligned; H in 1..128.  |q| below 2^-14 of its
  *          head's largest loses bits: at most 2^-22 of that largest.
