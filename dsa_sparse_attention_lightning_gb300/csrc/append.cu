@@ -135,7 +135,8 @@ append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
         const float is = s > 0.f ? 1.f / s : 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * h + i] *= is;
-        reinterpret_cast<uint32_t*>(row)[32 * h + lane] = e2m1x8(v + 8 * h);
+        // (a negative value times 0 would be the code of -0)
+        reinterpret_cast<uint32_t*>(row)[32 * h + lane] = is > 0.f ? e2m1x8(v + 8 * h) : 0;
         if (lane % 2 == 0) row[kNvCodeBytes + 16 * h + lane / 2] = sb;
       }
     } else {
