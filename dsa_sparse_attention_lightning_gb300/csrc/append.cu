@@ -53,6 +53,14 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   return r;
 }
 
+// x / d rounded to nearest, from rd = 1 / d rounded to nearest: one correction of the product by its
+// exact remainder (P. Markstein, IBM J. Res. Dev. 34, 1990), which is taken negative so that 0 keeps
+// its sign.  Infinities and NaN are the product's.
+__device__ __forceinline__ float quotient(float x, float d, float rd) {
+  const float q = x * rd, c = fmaf(-fmaf(q, d, -x), rd, q);
+  return fabsf(q) < INFINITY ? c : q;
+}
+
 __device__ __forceinline__ float bf16_val(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);
 }
@@ -133,8 +141,10 @@ append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
         const uint8_t sb = __nv_cvt_float_to_fp8(amax / 6.f, __NV_SATFINITE, __NV_E4M3);
         const float s = e4m3_to_float(sb);
         const float is = s > 0.f ? 1.f / s : 0.f;
+        // quotients: the product with 1 / s would move values off the middle between two codes.  Divisions
+        // take 5.4 us for 4096 tokens (in L2, with FP4 keys), these 5.0, products 4.9
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * h + i] *= is;
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = quotient(v[8 * h + i], s, is);
         // (a negative value times 0 would be the code of -0)
         reinterpret_cast<uint32_t*>(row)[32 * h + lane] = is > 0.f ? e2m1x8(v + 8 * h) : 0;
         if (lane % 2 == 0) row[kNvCodeBytes + 16 * h + lane / 2] = sb;

@@ -43,3 +43,24 @@ def test_codes_of_a_block_whose_scale_is_zero(dsa):
     x[2, ::3] = -1e-30
     row = append(dsa, x, 1.0, True)
     assert (row[:, :288] == 0).all()
+
+
+def test_values_half_way_between_two_fp4_codes(dsa):
+    """v / scale at every midpoint of E2M1, for every scale: the even code, whatever 1 / scale rounds to."""
+    mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=DEV)
+    even = torch.tensor([0, 2, 2, 4, 4, 6, 6], device=DEV)                     # codes of 0, 1, 1, 2, 2, 4, 4
+    code = torch.arange(1, 0x7F, device=DEV, dtype=torch.uint8)                # all scales but 0 and NaN
+    scale = code.view(torch.float8_e4m3fn).float()
+    blocks = torch.zeros(128, 16, device=DEV)
+    # 6, the midpoints, their negatives: exact in bf16 (a scale has 4 bits, a midpoint 3)
+    blocks[:126, 0] = 6 * scale
+    blocks[:126, 1:8] = mid * scale[:, None]
+    blocks[:126, 8:15] = -mid * scale[:, None]
+    x = torch.zeros(4, 576, dtype=torch.bfloat16, device=DEV)
+    x[:, :512] = blocks.view(4, 512).to(torch.bfloat16)
+    assert torch.equal(x[:, :512].float().view(128, 16), blocks)
+    row = append(dsa, x, 1.0, True)
+    assert torch.equal(row[:, 256:288].reshape(-1)[:126], code)
+    el = nibbles(row[:, :256]).view(128, 16)[:126].long()
+    assert (el[:, 0] == 7).all()
+    assert (el[:, 1:8] == even).all() and (el[:, 8:15] == even + 8).all()
