@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kAppWarps * 32)
 append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
                  const float* __restrict__ lat_gamma, float lat_eps,
                  const double* __restrict__ inv_freq, float mscale, int interleaved,
-                 float inv_scale, const uint16_t* __restrict__ k_raw, int64_t k_row,
+                 float latent_scale, float inv_scale, const uint16_t* __restrict__ k_raw, int64_t k_row,
                  const float* __restrict__ key_gamma, const float* __restrict__ key_beta,
                  float key_eps, const int32_t* __restrict__ block_table, int B, int max_pages,
                  const int32_t* __restrict__ tok_req, const int32_t* __restrict__ tok_pos, int T,
@@ -107,9 +107,8 @@ append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
       v[2 * i + 1] = bf16_hi(w[i]);
       sq = fmaf(v[2 * i], v[2 * i], fmaf(v[2 * i + 1], v[2 * i + 1], sq));
     }
-    float f = inv_scale;
     if (lat_gamma) {
-      f *= rsqrtf(warp_sum(sq) / (float)kVDim + lat_eps);
+      const float f = inv_scale * rsqrtf(warp_sum(sq) / (float)kVDim + lat_eps);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 g = reinterpret_cast<const float4*>(lat_gamma + 256 * (i >> 1))[2 * lane + (i & 1)];
@@ -117,11 +116,12 @@ append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= f;
+      for (int i = 0; i < 16; ++i) v[i] = quotient(v[i], latent_scale, inv_scale);   // as dsa_write_kv
     }
     float2 r = make_float2(xa, xb);
     if (inv_freq) r = rotate(xa, xb, rotation(fraction, pos, mscale));
-    const uint32_t rr = pack_e4m3x4(r.x * inv_scale, r.y * inv_scale, 0.f, 0.f);
+    const uint32_t rr = pack_e4m3x4(quotient(r.x, latent_scale, inv_scale),
+                                    quotient(r.y, latent_scale, inv_scale), 0.f, 0.f);
     if (page < 0 || (int64_t)page >= num_pages) {
       if (lane == 0) raise_dev(status, DSA_DEV_BAD_PAGE);
       continue;
@@ -174,7 +174,7 @@ cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t st) {
   auto go = [&](auto kernel) {
     kernel<<<grid, kAppWarps * 32, 0, st>>>(
         static_cast<const uint16_t*>(a.latent), a.lat_row, a.lat_gamma, a.lat_eps, a.inv_freq,
-        a.mscale, a.interleaved ? 1 : 0, 1.f / a.latent_scale,
+        a.mscale, a.interleaved ? 1 : 0, a.latent_scale, 1.f / a.latent_scale,
         static_cast<const uint16_t*>(a.k_raw), a.k_row, a.key_gamma, a.key_beta, a.key_eps,
         a.block_table, a.B, a.max_pages, a.tok_req, a.tok_pos, a.T, a.key_cache, a.latent_cache,
         a.num_pages, a.status);

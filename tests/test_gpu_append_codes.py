@@ -64,3 +64,26 @@ def test_values_half_way_between_two_fp4_codes(dsa):
     el = nibbles(row[:, :256]).view(128, 16)[:126].long()
     assert (el[:, 0] == 7).all()
     assert (el[:, 1:8] == even).all() and (el[:, 8:15] == even + 8).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 7.0, 3.0, 0.3, 0.15, 0.011, 1.1, 13 / 64, 448 / 13, 1 / 448])
+def test_rows_without_norm_or_rotation_at_any_scale(dsa, scale):
+    """Every bf16 value: the bytes of dsa_write_kv, of quotients by the scale, in rows of either format; a
+    rotation at position 0 changes none of them."""
+    bits = torch.arange(65536, device=DEV).to(torch.int16)
+    x = torch.zeros(128, 576, dtype=torch.bfloat16, device=DEV)
+    x.view(-1)[:65536] = bits.view(torch.bfloat16)
+    x = x[torch.randperm(128, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)].contiguous()
+    row = append(dsa, x, scale, False)
+    kc = torch.zeros(2, 8448, dtype=torch.uint8, device=DEV)
+    lc = torch.zeros(2, PAGE, 576, dtype=torch.uint8, device=DEV)
+    pos = torch.arange(128, dtype=torch.int32, device=DEV)
+    dsa.dsa_write_kv(torch.zeros(128, 128, dtype=torch.bfloat16, device=DEV), torch.ones(128, device=DEV),
+                     torch.zeros(128, device=DEV), 1e-5, x, scale, torch.arange(2, dtype=torch.int32, device=DEV)[None],
+                     torch.zeros_like(pos), pos, kc, lc)
+    assert torch.equal(row, lc.view(-1, 576))
+    assert torch.equal(append(dsa, x, scale, True)[:, 288:], row[:, 512:])
+    finite = torch.nan_to_num(x, nan=1.0, posinf=1.0, neginf=-1.0)
+    still = torch.zeros(32, dtype=torch.float64, device=DEV)                  # no turn at any position
+    a, b = append(dsa, finite, scale, False)[:, 512:], append(dsa, finite, scale, False, still)[:, 512:]
+    assert torch.equal(a.view(torch.float8_e4m3fn).float(), b.view(torch.float8_e4m3fn).float())
