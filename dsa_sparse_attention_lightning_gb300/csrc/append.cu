@@ -15,11 +15,14 @@
 // of the warp 512 contiguous bytes; two lanes an NVFP4 block) and RoPE pair l.  Every load of
 // a token but its page number is issued before any is used, and the page number is waited for
 // behind the norm and the rotation.  CTAs of four warps, at most eight per SM (a warp takes
-// several tokens then): 16383 latent rows 6.3 us (4.5 TB/s; 7.6 with a CTA for every four, 8.1
-// with 16 consecutive dims per lane), 4096 tokens into MXFP4 + NVFP4 4.6 us, 64 into FP8 2.6 us.
-// These are of inputs in L2; from HBM 16383 rows take 8.5 us, 100000 35.6 (4.9 TB/s).  Kept values and
-// looked-up pages were slower (7.3, 6.5), and so were fewer registers for more warps (9.3 cold); rows
-// prefetched by cp.async gain 7 % without an index key and lose 4 % with one.
+// several tokens then), and no variant may have more than the 64 registers that this leaves: with 72 and
+// seven CTAs 100000 tokens with FP8 keys and NVFP4 rows take 91 us instead of 72, with MXFP4 keys and
+// FP8 rows 78 instead of 64.
+// Measured, inputs not in L2: 64 tokens with FP8 keys and rows 2.7 us, 4096 with MXFP4 keys and NVFP4
+// rows 5.1, 16383 latent rows 8.7, 100000 37.5 (4.6 TB/s); with FP8 keys 57.6, with MXFP4 keys and NVFP4
+// rows 78.  A CTA for every four tokens, 16 consecutive dims per lane, kept values, looked-up pages
+// and fewer registers for more warps were slower (16383 rows of inputs in L2: 7.6, 8.1, 7.3 and 6.5
+// instead of 6.3; 9.3 cold); rows prefetched by cp.async gain 7 % without an index key and lose 4 % with one.
 #include "dsa_common.cuh"
 #include "rope_common.cuh"
 #include "write_common.cuh"
@@ -66,7 +69,7 @@ __device__ __forceinline__ float bf16_val(const uint16_t* p) {
 }
 
 template <int kKey, bool kNv>
-__global__ void __launch_bounds__(kAppWarps * 32)
+__global__ void __launch_bounds__(kAppWarps * 32, kAppCtasPerSm)
 append_kv_kernel(const uint16_t* __restrict__ latent, int64_t lat_row,
                  const float* __restrict__ lat_gamma, float lat_eps,
                  const double* __restrict__ inv_freq, float mscale, int interleaved,
