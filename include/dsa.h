@@ -384,7 +384,11 @@ int dsa_topk_dcp(const float* scores, int64_t ld, const int32_t* row_len, int R,
  * (vLLM post, "What Kimi K3.1 Pro changes": MLA attention runs exactly over
  * only the selected tokens; TokenSpeed post, "Sparse attention in Kimi K3.1
  * Pro": every attention head attends to the selected tokens.)  A row with no
- * valid token gets out = 0 and lse = -inf.
+ * valid token gets out = 0 and lse = -inf.  A weight below 2^-14 of the largest
+ * among the tokens of the same split is counted in lse but not in out: tails of
+ * equal weights 9.75 nats under one token, 0.107 of the mass of 2048 tokens, lose
+ * 0.007 in calls of up to 16 rows and all of it in calls of 256 (one split each);
+ * dsa_mla_decode has no such floor.
  *
  *  q       bf16 [R][H][576]; H in {16, 32, 64, 128}.
  *  idx     int32 [R][k], k in 1..2048 (e.g. the output of dsa_topk).
