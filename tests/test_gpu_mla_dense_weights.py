@@ -227,3 +227,21 @@ def test_a_row_is_the_same_beside_any_others(dsa):
     # values 0 and 1: twice the bound of `held` is below 2 * (2^-8 + 2^-9 + 2^-11 + 2^-12 + 2^-13) < 2^-6
     assert ((a[0].double() - b[199].double()).abs() <= 2.0 ** -6).all()
     held(a, call(dsa, alone)[1], s, 0, longest_range(1, 1, 16, n))
+
+
+@pytest.mark.parametrize("H", [5, 64])
+def test_a_context_that_begins_with_pages_that_are_skipped(dsa, H):
+    """Bad pages at the front of every context and at its end: no reference before the first visible token."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(19)
+    n = 40 * PAGE
+    steer = torch.rand(n, generator=g, device=DEV) * 4 + 30
+    s = steered(steer, 1 + torch.randn(n, 512, generator=g, device=DEV), strengths(H, 8.0, 8.0), 20, 12, 2)
+    good = {**s, "bt": s["bt"][:, 3:39].contiguous(), "len": s["len"] - 4 * PAGE}
+    s["bt"][:, :3] = torch.tensor([-1, 40, 10 ** 6], dtype=torch.int32, device=DEV)
+    s["bt"][:, 39] = -7
+    ws = torch.empty(dsa.mla_decode_workspace_size(24, H), dtype=torch.uint8, device=DEV)
+    out, lse = call(dsa, s, workspace=ws)
+    assert dsa.check_device_status(ws) == 2
+    for row in (0, 23):
+        held(out, lse, good, row, longest_range(12, 2, H, n))
